@@ -259,6 +259,8 @@ __device__ void rows_scale_role(const KvAttnParams& p, uint32_t sbase, const Row
       const int64_t at = ((int64_t)pg * p.Hk + rs.s.hk) * p.s.page_size + off;
       ks = __ldg(reinterpret_cast<const float2*>(p.k_scale + at));
       vs = __ldg(reinterpret_cast<const float2*>(p.v_scale + at));
+      // what a page holds past the last key must not enter the block's bounds
+      if (key + 1 >= rs.s.len) ks.y = vs.y = 0.f;
     };
     scales(0, page(0));
     int pg = page(1);
@@ -266,8 +268,9 @@ __device__ void rows_scale_role(const KvAttnParams& p, uint32_t sbase, const Row
       const int s = blk % C::SCR;
       if (!sy.wt.wait_warp(sy.bar(C::kBarScaleEmpty + s), ((blk / C::SCR) & 1u) ^ 1u, 0x3d)) return;
       const uint32_t dst = sbase + C::kOffScale + s * 1024u + idx * 8;
-      st_shared_f2(dst, make_float2(ks.x * p.c, ks.y * p.c));
-      st_shared_f2(dst + 512, vs);
+      // + 0: a scale of -0 becomes 0 (the bounds compare bits)
+      st_shared_f2(dst, make_float2(fmaf(ks.x, p.c, 0.f), fmaf(ks.y, p.c, 0.f)));
+      st_shared_f2(dst + 512, make_float2(vs.x + 0.f, vs.y + 0.f));
       __syncwarp();
       if (lead) ptx::mbar_arrive(sy.bar(C::kBarScale + s));
       scales(i + 1, pg);
