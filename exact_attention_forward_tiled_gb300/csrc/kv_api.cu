@@ -207,6 +207,7 @@ int attention(const void* q, const void* k_cache, const void* v_cache, const flo
   if (B == 0 || Sq == 0 || (cu_seqlens_q != nullptr && total_q == 0)) return FA_OK;
   if (B > kMaxSeqs) return FA_ERR_UNSUPPORTED;
   const int total = cu_seqlens_q != nullptr ? total_q : B * Sq;
+  Sq = std::min(Sq, total);   // a loose bound on the rows of a packed sequence
   if (prefix_len > 0 && !prefix_pages) return FA_ERR_INVALID_ARG;
   if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(prefix_pages, 4)) return FA_ERR_ALIGNMENT;
@@ -224,10 +225,10 @@ int attention(const void* q, const void* k_cache, const void* v_cache, const flo
   if (workspace == nullptr || workspace_bytes < z.bytes) return FA_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return FA_ERR_ALIGNMENT;
   // the work lines are counted in 32 bits
-  const int64_t own_units = (int64_t)B * ((Sq * G + z.own.rt - 1) / z.own.rt) *
-                            (((int64_t)max_pages * page_size + z.own.unit - 1) / z.own.unit);
+  const int64_t own_tiles = std::min((int64_t)B * ((Sq * G + z.own.rt - 1) / z.own.rt), total * G / z.own.rt + B);
+  const int64_t own_units = own_tiles * (((int64_t)max_pages * page_size + z.own.unit - 1) / z.own.unit);
   const int64_t pre_units = z.prefix_tiles * (((int64_t)prefix_len + z.pre.unit - 1) / z.pre.unit);
-  if (own_units + pre_units > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  if (own_units + pre_units >= INT32_MAX) return FA_ERR_UNSUPPORTED;
 
   fa::KvMergeParams M;
   std::memset(&M, 0, sizeof(M));
@@ -247,6 +248,7 @@ int attention(const void* q, const void* k_cache, const void* v_cache, const flo
   P.prefix_pages = prefix_pages;
   P.prefix_len = prefix_len;
   P.direct = !prefix;
+  P.most_units = (int)own_units;
   char* ws = static_cast<char*>(workspace);
   P.cum = reinterpret_cast<int*>(ws + z.off_cum);
   fa::KvAttnLaunch L;
@@ -403,6 +405,7 @@ size_t fa_fwd_kvcache_workspace_size(int B, int Hq, int Hk, int Sq, int D, int t
   Shape z;
   const int64_t total = total_q > 0 ? total_q : (int64_t)B * Sq;
   if (total > INT32_MAX) return 0;
+  Sq = (int)std::min<int64_t>(Sq, total);
   // enough for 8-bit and 16-bit caches
   size_t most = 0;
   for (int eb = 1; eb <= 2; ++eb) {

@@ -83,6 +83,7 @@ struct KvAttnParams {
   int prefix_tiles;         // row tiles of the prefix, 0 if it is no part of this launch
   int ranges;               // of the work line; workers: ranges * Hk
   int pass_own;             // the sequences' own keys are part of this launch's work line
+  int most_units;           // of the sequences' own keys, for any lengths and row counts within their bounds
   int direct;               // an item that one worker holds whole is written to O and LSE (no prefix to join)
   int box_rows;             // rows of a TMA box of the cache
   // workspace

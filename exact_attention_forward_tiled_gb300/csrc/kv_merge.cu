@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) kv_merge_kernel(const _
     const int rt = mp.own.rt;
     const int R = (t - w.first) * p.G + gq;
     const int mt = R / rt;
+    // what is not on the line has no partials (sequences that overlap)
+    if (__ldg(p.cum + b + 1) - __ldg(p.cum + b) != w.mtiles * w.units) return;
     own_r = R - mt * rt;
     own = partials_of(mp.own.pre_total + __ldg(p.cum + b) + mt * w.units, w.units, mp.own.ranges, mp.own.pre_total + own_U,
                       mp.own.whole + whole_slot(p, rt, b, w.first, mt));

@@ -106,36 +106,42 @@ __device__ __forceinline__ KvSegment find_segment(const KvAttnParams& p, int rt,
 }
 
 // Units before each sequence, cum[0 .. B], by a scan over the block (all its
-// threads; sm_warp: one int per warp). Ends with a barrier.
+// threads; sm_warp: one int per warp). Ends with a barrier. Valid sequences have
+// at most p.most_units (counted in 32 bits): all of them together have no more
+// rows than `total`. Sequences that overlap (prefix sums that go down in between)
+// can have more; sums stop one above, and then nothing is done and it is reported.
 __device__ __forceinline__ void scan_units(const KvAttnParams& p, int rt, int unit, int threads, int* cum, int* sm_warp) {
+  const uint32_t most = (uint32_t)p.most_units;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = threads >> 5;
-  int carry = 0;
+  uint32_t carry = 0;
   for (int b0 = 0; b0 < p.s.B; b0 += threads) {
     const int b = b0 + threadIdx.x;
-    int v = 0;
+    uint32_t x = 0;
     if (b < p.s.B) {
       const SeqWork w = seq_work(p, b, rt, unit);
-      v = w.mtiles * w.units;
+      x = min((uint32_t)(w.mtiles * w.units), most + 1u);
       if (w.bad && blockIdx.x == 0) atomicOr(p.s.status, kDevBadSeqlens);
     }
-    int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = min(x + y, most + 1u);
     }
-    if (lane == 31) sm_warp[warp] = x;
+    if (lane == 31) sm_warp[warp] = (int)x;
     __syncthreads();
-    int before = carry, all = 0;
+    uint32_t before = carry;
     for (int i = 0; i < warps; ++i) {
-      if (i < warp) before += sm_warp[i];
-      all += sm_warp[i];
+      if (i < warp) before = min(before + (uint32_t)sm_warp[i], most + 1u);
+      carry = min(carry + (uint32_t)sm_warp[i], most + 1u);
     }
-    if (b < p.s.B) cum[b] = before + x - v;
-    carry += all;
+    if (b < p.s.B) cum[b + 1] = (int)min(before + x, most + 1u);
     __syncthreads();
   }
-  if (threadIdx.x == 0) cum[p.s.B] = carry;
+  if (threadIdx.x == 0) cum[0] = 0;
+  if (carry > most) {   // the same in every thread
+    for (int b = threadIdx.x; b <= p.s.B; b += threads) cum[b] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.s.status, kDevBadSeqlens);
+  }
   __syncthreads();
 }
 

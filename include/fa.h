@@ -410,7 +410,9 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const int* p
  * [0, num_pages) is not dereferenced (its rows read as zeros and are not
  * written); both are reported as FA_ERR_DEVICE_SEQLENS by
  * fa_get_device_status. Rows of a packed tensor past cu_seqlens[B] are left
- * as they were. Cache rows at or past a sequence's length may hold anything.
+ * as they were. Where prefix sums go down, sequences overlap: their rows are
+ * undefined, and attention that would be more work than total_q rows can be is
+ * not done (reported). Cache rows at or past a sequence's length may hold anything.
  */
 
 /*
