@@ -925,5 +925,6 @@ def attention_forward_prefix(q, cache, prefix_pages, prefix_len, block_table, se
     page_size)]``): these are read once for the whole batch. block_table and
     seqlens_k name each sequence's own keys, which follow."""
     _need(prefix_len >= 0, "prefix_len must not be negative")
+    _need(prefix_pages is not None or prefix_len == 0, "a prefix needs prefix_pages")
     return _attention_kvcache(q, cache, prefix_pages, prefix_len, block_table, seqlens_k, causal, scale, cu_seqlens_q,
                               max_seqlen_q, out, lse, workspace, stream)
