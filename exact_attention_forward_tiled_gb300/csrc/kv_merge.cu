@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) kv_merge_kernel(const _
   wait_for_predecessor();
   if (w.bad || t < w.first || t >= w.first + w.n) return;
   const int hk = h / p.G, gq = h - hk * p.G;
-  const int own_U = __ldg(p.cum + p.s.B);
+  // (plain loads: the kernel before wrote it, perhaps while this one was resident)
+  const int own_U = p.cum[p.s.B], cum_b = p.cum[b];
 
   Partials own, pre{0, 0, 0, 0, 0, 0};
   int own_r, pre_r = 0;
@@ -70,9 +71,9 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) kv_merge_kernel(const _
     const int R = (t - w.first) * p.G + gq;
     const int mt = R / rt;
     // what is not on the line has no partials (sequences that overlap)
-    if (__ldg(p.cum + b + 1) - __ldg(p.cum + b) != w.mtiles * w.units) return;
+    if (p.cum[b + 1] - cum_b != w.mtiles * w.units) return;
     own_r = R - mt * rt;
-    own = partials_of(mp.own.pre_total + __ldg(p.cum + b) + mt * w.units, w.units, mp.own.ranges, mp.own.pre_total + own_U,
+    own = partials_of(mp.own.pre_total + cum_b + mt * w.units, w.units, mp.own.ranges, mp.own.pre_total + own_U,
                       mp.own.whole + whole_slot(p, rt, b, w.first, mt));
     if (own.n == 1 && p.prefix_tiles == 0) return;   // finished by the worker that had all of it
   }
