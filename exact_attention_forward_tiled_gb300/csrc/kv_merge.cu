@@ -31,7 +31,7 @@ struct Partials {
 
 __device__ __forceinline__ Partials partials_of(int ua, int units, int ranges, int U, int whole) {
   Partials q{0, ua, whole, 0, min(ranges, U), U};
-  if (units == 0) return q;
+  if (units == 0 || U == 0) return q;
   q.ca = range_of(ua, q.ranges, U);
   q.n = range_of(ua + units - 1, q.ranges, U) - q.ca + 1;
   return q;
@@ -70,8 +70,6 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) kv_merge_kernel(const _
     const int rt = mp.own.rt;
     const int R = (t - w.first) * p.G + gq;
     const int mt = R / rt;
-    // what is not on the line has no partials (sequences that overlap)
-    if (p.cum[b + 1] - cum_b != w.mtiles * w.units) return;
     own_r = R - mt * rt;
     own = partials_of(mp.own.pre_total + cum_b + mt * w.units, w.units, mp.own.ranges, mp.own.pre_total + own_U,
                       mp.own.whole + whole_slot(p, rt, b, w.first, mt));
@@ -85,6 +83,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) kv_merge_kernel(const _
     pre_r = R - mt * rt;
     pre = partials_of(mt * units, units, mp.pre.ranges, mp.pre.pre_total + (mp.pre.own ? own_U : 0), mp.pre.whole + mt);
   }
+  if (own.n == 0 && w.units > 0) return;   // the line was not worked through (scan_units)
   const int n = own.n + pre.n;
   // row of partial i in its launch's part of the workspace
   auto at = [&](int i) -> int64_t {

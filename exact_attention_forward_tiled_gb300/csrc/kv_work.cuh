@@ -131,7 +131,7 @@ __device__ __forceinline__ void scan_units(const KvAttnParams& p, int rt, int un
     __syncthreads();
     uint32_t before = carry;
     for (int i = 0; i < warps; ++i) {
-      if (i < warp) before = min(before + (uint32_t)sm_warp[i], most + 1u);
+      if (i == warp) before = carry;
       carry = min(carry + (uint32_t)sm_warp[i], most + 1u);
     }
     if (b < p.s.B) cum[b + 1] = (int)min(before + x, most + 1u);
