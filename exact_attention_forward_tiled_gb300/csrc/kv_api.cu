@@ -88,11 +88,15 @@ struct Shape {
 // each; the many-row kernel reads them once for up to 256 rows, and pays for
 // 128. 16-bit caches change at 16 rows, 8-bit caches, whose codes it has to
 // convert for 128 rows however few there are, at 32. Measured, few-row against
-// many-row kernel, B = 64, 8 K/V heads, up to 8192 keys:
-//   16-bit, D = 128: 16 rows 237, 281 us; 24 rows 433, 293; 64 rows 855, 326
-//   16-bit, D = 64, 20 rows: 224, 201; D = 256, 20 rows: 777, 750
-//   e4m3, D = 128: 16 rows 187, 316; 32 rows 355, 332; 36 rows 503, 336
-//   int8, 32 rows: D = 64 206, 314; D = 256 590, 746
+// many-row kernel, B = 64, 8 K/V heads, 2048 to 8192 keys:
+//   16-bit, D = 128: 16 rows 223, 268 us; 20 rows 412, 275; 64 rows 815, 290
+//   16-bit, 20 rows: D = 64 205, 189; D = 256 754, 736
+//   e4m3, D = 128: 16 rows 134, 299; 32 rows 251, 304; 36 rows 357, 304
+//   e4m3, 32 rows: D = 64 165, 287; D = 256 522, 703; 36 rows: 234, 288; 761, 704
+//   int8, 32 rows: D = 64 183, 293; D = 128 280, 312; D = 256 567, 727
+//   int8, 36 rows: D = 64 260, 294; D = 128 403, 313; D = 256 829, 728
+// (one bound for all head sizes: at D = 64 the 8-bit few-row kernel would still
+// win up to 48 rows)
 // `rows` bounds an item's rows, `mean` is what they are on average: that is
 // what the few-row kernel's time goes with (24 packed sequences of 4 to 20
 // rows, 12 on average, 16-bit, D = 256: 133, 208 us).
@@ -122,8 +126,8 @@ bool shape_of(Shape& z, int B, int Hq, int Hk, int S, int D, int elem_bytes, int
   const int64_t rows_own = (int64_t)S * G, rows_pre = (int64_t)total * G;
   // A prefix that more than 32 rows share gets a pass of its own; fewer rows go
   // on one work line with the sequences' own keys, with the few-row kernel (e4m3,
-  // 32768 shared keys, up to 1024 own ones: 48 rows 57 us split, 68 on one line;
-  // 32 rows 55 and 63, but with 100 own and 300 shared keys 20 and 16).
+  // 32768 shared keys, up to 1024 own ones: 48 rows 53 us split, 58 on one line;
+  // 32 rows 48 and 43, and with 100 own and 300 shared keys 19 and 15).
   z.split = prefix && rows_pre > 32;
   const bool one_line = prefix && !z.split;
   choose(z.own, one_line ? rows_pre : rows_own, (rows_pre + B - 1) / B, Hk, D, elem_bytes,

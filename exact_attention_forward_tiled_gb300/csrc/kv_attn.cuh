@@ -5,7 +5,7 @@
 // Row (i, g) of a work item is query token i of head hk * G + g: the G query
 // heads that share a K/V head and all query tokens of a sequence (or, for the
 // shared prefix, of all sequences) are rows of one matrix product, so K and V
-// are read once for all of them.
+// are read once for every 16 of them.
 //
 //   x_ij = (q_i . kcode_j) ks_j scale log2 e,  p_ij = 2^(x_ij - m_i),
 //   l_i = sum_j p_ij,  O_i = (sum_j p_ij vs_j vcode_j) / l_i,
@@ -21,22 +21,18 @@
 // operands as 16-bit tiles in shared memory, which an 8-bit cache does not
 // give; here the codes go from shared memory to registers and become f16 there.
 //
-// Arithmetic with an 8-bit cache. Scores, int8: f16 products, where every code
-// is exact; query rows are scaled by a power of two so that their largest
-// element is in [2^14, 2^15) (bf16 queries; fp16 ones are taken as they are):
-// exact but for elements below 2^-38 of the row's largest. Scores, e4m3: e4m3
-// products on the codes as they lie in the cache (no conversion, and twice the
-// depth per instruction in about half the time: 4.5 cycles for a depth of 32
-// against 8 for 16); a query row, scaled so that its largest element is in
-// [2^7, 2^8), is the sum of two e4m3 numbers per element (bf16 queries: 8 bits)
-// or three (fp16: 11 bits), exact but for elements that need bits below 2^-9:
-// those are off by up to 2^-10, 2^-17 of the row's largest. Accumulation is
-// fp32. The second product runs in f16, where the codes are exact. The weights
-// p vs, whose range is that of the V scales, are held at a power of
-// two per row, 2^lr, chosen such that the largest is about 2^6 and none
-// reaches 2^16, and rounded to f16 (11 bits). 2^lr sits in the exponent's
-// argument, so O and l both carry it; it moves only when it has to. l takes
-// the unrounded p.
+// Arithmetic with an 8-bit cache. Both products run in f16, where every code is
+// exact, with fp32 accumulation. Query rows are scaled by a power of two so that
+// their largest element is in [2^14, 2^15) (bf16 queries; fp16 ones are taken as
+// they are): every element is held to 2^-38 of the row's largest. (e4m3 products
+// on the raw codes, a query as the sum of two or three e4m3 numbers per element,
+// lose what lies below 2^-17 of the largest, and are slower where it counts: 8
+// rows 124 against 123 us, 16 rows 172 against 134, B = 64 of 2048 .. 8192 keys,
+// 8 heads of 128.) The weights p vs, whose range is that of the V scales, are
+// held at a power of two per row, 2^lr, lr <= 100, chosen such that the largest
+// is about 2^6 and none reaches 2^16, and rounded to f16 (11 bits). 2^lr sits in
+// the exponent's argument, so O and l both carry it; it moves only when it has
+// to. l takes the unrounded p.
 //
 // Work split. The keys of every (sequence, K/V head, row tile) are cut into
 // tiles of 16 or 32 keys; all tiles form one line, cut into equal contiguous
@@ -96,9 +92,7 @@ struct KvCfg {
   static constexpr int MT = KT / 16, OT = D / 16, QS = D / 16;
   static constexpr int kThreads = 32 * W;
   static constexpr float kTau = 8.f;
-  static constexpr bool kE4 = KIND == kCacheE4M3;            // scores by e4m3 products
-  // Q fragments, 4 bytes each: of a k16 step two (16-bit), of a k32 step and part two (e4m3, three parts)
-  static constexpr int QW = kE4 ? 3 * (D / 16) : D / 8;
+  static constexpr int QW = D / 8;                           // Q fragments, 4 bytes each: two of a k16 step
   static constexpr bool kQRegs = D * NB <= 128;              // they are in registers, else in shared memory
   static constexpr int SR = NS <= 4 ? 2 : 4;                 // tiles whose scales are held
   static constexpr int SEGS = 4;                             // segments found ahead: at most (NS - 1) / 2 + 2 are open
@@ -126,24 +120,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_16832_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// four numbers below 2^8 -> their e4m3 codes, and what is left of them
-__device__ __forceinline__ uint32_t take_e4m3(float (&x)[4]) {
-  const uint32_t w = ptx::pack_e4m3x4(x[0], x[1], x[2], x[3]);
-  uint32_t lo, hi;
-  codes_to_f16<kCacheE4M3>(w, lo, hi);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  x[0] -= a.x;
-  x[1] -= a.y;
-  x[2] -= b.x;
-  x[3] -= b.y;
-  return w;
 }
 // 8 x 8 matrix of 16-bit elements, two per thread, transposed across the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -313,9 +289,8 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
     min_lim = __reduce_min_sync(0xffffffffu, min_lim);
 
     // ---- Q fragments: row g of each eight, the elements of this thread's
-    // chunks in order (box, chunk, element), four (f16: two words, e4m3: a word
-    // of each part) at a time; and the rows' factors: the scores of a row are
-    // its products times rowf
+    // chunks in order (box, chunk, element), four (two words) at a time; and the
+    // rows' factors: the scores of a row are its products times rowf
     uint32_t qf[C::kQRegs ? NB : 1][C::QW];
     float rowf[NB][2];
 #pragma unroll
@@ -336,58 +311,32 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
         v[s + 1] = make_uint2(x.z, x.w);
         m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
       }
-      float qs = 1.f, f = 1.f;
-      if (C::kE4 || (C::k8 && p.q_bf16)) {
+      float qs = 1.f;
+      if (C::k8 && p.q_bf16) {
         uint32_t e = max(m & 0xffffu, m >> 16);
         e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
         e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-        const float amax = p.q_bf16 ? __uint_as_float(e << 16) : __half2float(__ushort_as_half((unsigned short)e));
-        const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-        if (ex != -127 && ex != 128) {
-          // the largest element times 2^sh is in [2^7, 2^8) or [2^14, 2^15)
-          // (less where it is below 2^-100); sh in [-120, 114]
-          const int sh = min((C::kE4 ? 7 : 14) - ex, 114);
+        float f = 1.f;
+        if (e != 0 && e < 0x7f80u) {
+          // the largest element times 2^sh is in [2^14, 2^15) (less where it is
+          // below 2^-100); sh in [-113, 114]
+          const int sh = min(14 - ((int)(e >> 7) - 127), 114);
           f = __uint_as_float((uint32_t)(127 + sh) << 23);
           qs = __uint_as_float((uint32_t)(127 - sh) << 23);
         }
-        // e4m3 parts hold no infinity: a row with one gets NaN, as its products would
-        if (C::kE4 && ex == 128) qs = CUDART_NAN_F;
-      }
-      uint32_t w[C::QW];
 #pragma unroll
-      for (int s = 0; s < C::QS; ++s) {
-        if (C::kE4) {
-          float x[4];
-          const uint32_t u[2] = {v[s].x, v[s].y};
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (p.q_bf16) {
-              x[2 * k] = __uint_as_float(u[k] << 16) * f;
-              x[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u) * f;
-            } else {
-              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&u[k]));
-              x[2 * k] = h.x * f;
-              x[2 * k + 1] = h.y * f;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 3; ++k) w[C::kE4 ? k * C::QS + s : 0] = take_e4m3(x);
-        } else {
-          if (C::k8 && p.q_bf16) {
-            v[s].x = ptx::pack_f16(__uint_as_float(v[s].x << 16) * f, __uint_as_float(v[s].x & 0xffff0000u) * f);
-            v[s].y = ptx::pack_f16(__uint_as_float(v[s].y << 16) * f, __uint_as_float(v[s].y & 0xffff0000u) * f);
-          }
-          w[C::kE4 ? 0 : 2 * s] = v[s].x;
-          w[C::kE4 ? 0 : 2 * s + 1] = v[s].y;
+        for (int s = 0; s < C::QS; ++s) {
+          v[s].x = ptx::pack_f16(__uint_as_float(v[s].x << 16) * f, __uint_as_float(v[s].x & 0xffff0000u) * f);
+          v[s].y = ptx::pack_f16(__uint_as_float(v[s].y << 16) * f, __uint_as_float(v[s].y & 0xffff0000u) * f);
         }
       }
 #pragma unroll
-      for (int s = 0; s < C::QW; s += 2) {
+      for (int s = 0; s < C::QS; ++s) {
         if (C::kQRegs) {
-          qf[C::kQRegs ? b : 0][s] = w[s];
-          qf[C::kQRegs ? b : 0][s + 1] = w[s + 1];
+          qf[C::kQRegs ? b : 0][2 * s] = v[s].x;
+          qf[C::kQRegs ? b : 0][2 * s + 1] = v[s].y;
         } else {
-          sts64(qbuf + ((b * (C::QW / 2) + s / 2) * 32 + lane) * 8, make_uint2(w[s], w[s + 1]));   // read back by the same lane
+          sts64(qbuf + ((b * C::QS + s) * 32 + lane) * 8, v[s]);   // read back by the same lane
         }
       }
       rowf[b][0] = C::k8 ? __shfl_sync(0xffffffffu, qs, 8 * c) : p.c;
@@ -395,7 +344,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
     }
     auto q_words = [&](int b, int s) -> uint2 {   // fragments 2 s, 2 s + 1
       return C::kQRegs ? make_uint2(qf[C::kQRegs ? b : 0][2 * s], qf[C::kQRegs ? b : 0][2 * s + 1])
-                       : lds64(qbuf + ((b * (C::QW / 2) + s) * 32 + lane) * 8);
+                       : lds64(qbuf + ((b * C::QS + s) * 32 + lane) * 8);
     };
 
     // ---- the warp's online softmax over its tiles
@@ -443,26 +392,17 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
               kw[t][r] = lds128(kbuf + bx * C::kBoxBytes + (16 * t + 8 * r + g) * RB + chunk * 16);
             }
 #pragma unroll
-          for (int st = 0; st < C::SPC; st += C::kE4 ? 2 : 1) {
+          for (int st = 0; st < C::SPC; ++st) {
             const int s = (bx * C::CH + ch) * C::SPC + st;
-            uint2 q[3][NB];   // e4m3: of each part
+            uint2 q[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              q[0][b] = q_words(b, C::kE4 ? s / 2 : s);
-              if (C::kE4) q[1][b] = q_words(b, (C::QS + s) / 2);
-              if (C::kE4 && !p.q_bf16) q[2][b] = q_words(b, (2 * C::QS + s) / 2);
-            }
+            for (int b = 0; b < NB; ++b) q[b] = q_words(b, s);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
               const uint32_t w0[4] = {kw[t][0].x, kw[t][0].y, kw[t][0].z, kw[t][0].w};
               const uint32_t w1[4] = {kw[t][1].x, kw[t][1].y, kw[t][1].z, kw[t][1].w};
               uint32_t a[4];
-              if (C::kE4) {
-                a[0] = w0[st & 3];
-                a[1] = w1[st & 3];
-                a[2] = w0[(st + 1) & 3];
-                a[3] = w1[(st + 1) & 3];
-              } else if (C::k8) {
+              if (C::k8) {
                 codes_to_f16<C::KIND>(w0[st], a[0], a[2]);
                 codes_to_f16<C::KIND>(w1[st], a[1], a[3]);
               } else {
@@ -472,15 +412,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
                 a[3] = w1[(2 * st + 1) & 3];
               }
 #pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                if (C::kE4) {
-                  mma_16832_e4m3(sc[t][b], a, q[0][b].x, q[0][b].y);
-                  mma_16832_e4m3(sc[t][b], a, q[1][b].x, q[1][b].y);
-                  if (!p.q_bf16) mma_16832_e4m3(sc[t][b], a, q[2][b].x, q[2][b].y);
-                } else {
-                  mma_16816(sc[t][b], a, q[0][b].x, q[0][b].y, C::KIND == kCacheBF16);
-                }
-              }
+              for (int b = 0; b < NB; ++b) mma_16816(sc[t][b], a, q[b].x, q[b].y, C::KIND == kCacheBF16);
             }
           }
         }

@@ -112,8 +112,9 @@ struct KvAttnGeom {
 // nb: query rows of an item / 8. As many warps as leave each the registers its
 // accumulators (D * nb / 4) and operands need: 12 in two CTAs (168 registers a
 // thread), or 8 or 6 in one (255). More warps with less spill in the inner loop
-// and lose: D = 128, nb = 1, e4m3, B = 64 of up to 8192 keys: 16 warps (128
-// registers) 143 us, 12 warps 116 us; nb = 2: 10 warps 207 us, 8 warps 176 us.
+// and lose, whole calls, D = 128, e4m3, B = 64 of 2048 .. 8192 keys: nb = 1, 16
+// warps (128 registers) 129 us, 12 warps 121 us; nb = 2, 10 warps 151 us, 8 warps
+// 134 us.
 constexpr KvAttnGeom kv_attn_geom(int D, int elem_bytes, int nb) {
   const int keys = D * elem_bytes <= 128 ? 32 : 16;
   const int slot = keys * D * elem_bytes;
@@ -121,7 +122,7 @@ constexpr KvAttnGeom kv_attn_geom(int D, int elem_bytes, int nb) {
   const int warps = D * nb >= 256 && slot <= 4096 ? 8 : 6;
   // 192 KB per SM for the rings and, where they are not in registers (D * nb >
   // 128), each warp's query fragments
-  const int q = D * nb > 128 ? nb * D * (elem_bytes == 1 ? 24 : 16) : 0;   // e4m3 in three parts, or 16 bits
+  const int q = D * nb > 128 ? nb * D * 16 : 0;
   int slots = (196608 / (ctas * warps) - q) / slot;
   slots = slots > 6 ? 6 : slots;
   return KvAttnGeom{ctas, warps, keys, slots};

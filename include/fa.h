@@ -470,8 +470,10 @@ int fa_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, c
  * Scores, softmax and sums are fp32. With a 16-bit cache the weights are
  * rounded to its type before they meet V, and keys that any query of the
  * sequence sees must be finite; with an 8-bit one both products run in f16,
- * where the codes are exact (a bf16 query row is held relative to its largest
- * element, to 2^-38 of it). Deterministic. Two kernels on `stream` (with a
+ * where the codes are exact: a bf16 query row is held to 2^-38 of its largest
+ * element (or to 2^-139, if that is more), the weights times their V scales are
+ * rounded to f16 (smaller ones to fewer bits where a row's V scales are all
+ * below 2^-94). Deterministic. Two kernels on `stream` (with a
  * prefix shared by more than 32 query rows per K/V head: three).
  */
 size_t fa_fwd_kvcache_workspace_size(int B, int Hq, int Hk, int Sq, int D, int total_q, int prefix_len);
