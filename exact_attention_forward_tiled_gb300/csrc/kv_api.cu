@@ -314,6 +314,22 @@ int move(bool append, void* const x[2], const long long* strides, void* k_cache,
   return cuda_status(launch(P, cache_kind(cache_dtype), dtype == FA_BF16, sms, static_cast<cudaStream_t>(stream)));
 }
 
+// Radians -> the fraction of a turn, in 2^-64 (whole turns per position change
+// nothing: positions are integers). 1 / 2 pi as the sum of two doubles, so that
+// the fraction is within one unit for |w| up to 2^40; one double alone leaves 53
+// bits, and positions of 2^31 off by 2^-25 turns.
+uint64_t turn_fraction(double w) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  const double a = std::fabs(w);
+  const double p = std::fma(a, kHi, 0.0);   // (a product could be fused with what follows)
+  const double rest = std::fma(a, kLo, std::fma(a, kHi, -p));   // a / 2 pi = p + rest
+  const double t = (p - std::floor(p)) * 0x1p64;
+  const uint64_t whole = (uint64_t)t;
+  const uint64_t u = std::fabs(rest) < 0.25 ? whole + (uint64_t)(int64_t)std::floor(t - (double)whole + rest * 0x1p64 + 0.5)
+                                            : whole + (uint64_t)((rest - std::floor(rest)) * 0x1p64);   // |w| past 2^50
+  return w < 0.0 ? 0 - u : u;
+}
+
 }  // namespace
 
 extern "C" {
@@ -333,11 +349,7 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const int* p
   for (int j = 0; j < rot_dim / 2; ++j) {
     if (axis[j] < 0 || axis[j] >= n_axes || !std::isfinite(inv_freq[j])) return FA_ERR_INVALID_ARG;
     P.axis[j] = (uint8_t)axis[j];
-    // radians -> turns -> the fraction of a turn, in 2^-64 (whole turns per
-    // position change nothing: positions are integers)
-    double f = inv_freq[j] / 6.283185307179586476925;
-    if (!(f >= 0.0 && f < 1.0)) f -= std::floor(f);
-    P.freq[j] = f >= 1.0 ? 0 : (uint64_t)(f * 18446744073709551616.0);
+    P.freq[j] = turn_fraction(inv_freq[j]);
   }
   if (T == 0 || (Hq == 0 && Hk == 0)) return FA_OK;
   if (!positions || (Hq > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out))) return FA_ERR_INVALID_ARG;

@@ -9,12 +9,12 @@
 // The map is orthogonal, so the backward pass is the same kernel with -phi.
 // Elements past rot_dim pass through.
 //
-// The angle is reduced exactly: the host gives w_j / 2 pi as a 64-bit binary
-// fraction of a turn, and the integer product p * fraction, modulo 2^64, is
-// the fraction of a turn left after all whole turns are dropped. A position of
-// 2^31 leaves an error of 2^-34 turns from the fraction's own rounding; an
-// fp32 product would be off by whole radians there. sincospif takes the upper
-// 32 bits.
+// The angle is reduced in integers: the host gives w_j / 2 pi as a 64-bit binary
+// fraction of a turn, rounded once, and the integer product p * fraction,
+// modulo 2^64, is the fraction of a turn left after all whole turns are dropped.
+// A position of 2^31 leaves an error of 2^-34 turns from the fraction's rounding;
+// an fp32 product would be off by whole radians there. sincospif takes the upper
+// 32 bits, which drops less than 2^-32 turns.
 //
 // HBM-bound: every element is read once and written once, 2 * 2 bytes. A CTA
 // takes a few tokens, computes their sines and cosines once into shared

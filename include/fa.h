@@ -366,8 +366,9 @@ int fa_bwd(const void* q, const void* k, const void* v, const void* o, const voi
  * Pair j of a head is (a, b); axis[j] names the axis whose position turns it:
  *   phi = positions[axis[j]][t] * inv_freq[j],
  *   a' = a cos phi - b sin phi,  b' = b cos phi + a sin phi.
- * The angle is reduced exactly for every int32 position; products and sums
- * are fp32, rounded once to the output type.
+ * The angle is reduced in integers, to within 2^-31 turns for every int32
+ * position (|inv_freq| up to 2^40); products and sums are fp32, rounded once to
+ * the output type.
  *
  *   q, k         [T, Hq, D], [T, Hk, D] 16-bit, by `strides`; H = 0 leaves a
  *                tensor out (its pointers may then be NULL)
