@@ -36,6 +36,7 @@ int check_cache(const void* k_cache, const void* v_cache, const float* k_scale, 
       (int64_t)B * max_pages > INT32_MAX || (cu == nullptr && (int64_t)B * S > INT32_MAX) ||
       (int64_t)Hk * D * 2 > INT32_MAX)
     return FA_ERR_INVALID_ARG;
+  if (cu != nullptr && B > 0 && S == 0 && total > 0) return FA_ERR_INVALID_ARG;   // rows, but no sequence may have any
   if (B == 0 || S == 0 || (cu != nullptr && total == 0)) return FA_OK;   // nothing to do
   if (!k_cache || !v_cache || !block_table || !seqlens_k) return FA_ERR_INVALID_ARG;
   if (k8 && (!k_scale || !v_scale)) return FA_ERR_INVALID_ARG;

@@ -1,7 +1,20 @@
-"""CPU tests of arguments that the binding has to refuse by itself."""
+"""CPU tests of arguments that the binding, or the C entry, refuses: a prefix
+without pages, packed rows with a bound of none."""
+import ctypes
+
 import pytest
+import torch
 
 from exact_attention_forward_tiled_gb300 import api
+from exact_attention_forward_tiled_gb300 import build as fa_build
+
+INVALID = -1
+
+
+@pytest.fixture(scope="module")
+def L():
+    fa_build.build()
+    return api.lib()
 
 
 def test_prefix_without_pages():
@@ -10,3 +23,28 @@ def test_prefix_without_pages():
         api.attention_forward_prefix(None, None, None, 5, None, None)
     with pytest.raises(ValueError, match="negative"):
         api.attention_forward_prefix(None, None, None, -1, None, None)
+
+
+def _append(L, B, S, cu, total):
+    return L.fa_kv_append(0x1000, 0x2000, 0x3000, 0x4000, 0x5000, 0x6000, 0x7000, 0x8000, B, 2, S, 128, 8, 16, 4, None, cu,
+                          total, api.FA_BF16, api.FA_FP8_E4M3, None)
+
+
+def _attn(L, B, S, cu, total):
+    return L.fa_fwd_kvcache(0x1000, 0x3000, 0x4000, 0x5000, 0x6000, 0x7000, 0x8000, 0xa000, 0xb000, B, 4, 2, S, 128, 8, 16, 4,
+                            ctypes.c_float(0.1), 1, cu, total, 0x10000, 1 << 40, api.FA_FP16, api.FA_INT8, None)
+
+
+@pytest.mark.parametrize("f", [_append, _attn])
+def test_rows_but_a_bound_of_none(L, f):
+    """Packed rows whose sequences may have none: not taken for nothing to do."""
+    assert f(L, 2, 0, 0x9000, 5) == INVALID
+    assert f(L, 2, 0, 0x9000, 0) == 0 and f(L, 0, 0, 0x9000, 5) == 0 and f(L, 2, 0, None, 0) == 0
+
+
+def test_rows_but_a_bound_of_none_from_python():
+    cu = torch.tensor([0, 2, 5], dtype=torch.int32)
+    for bound in (0, -1):
+        with pytest.raises(ValueError, match="max_seqlen_q"):
+            api._rows_per_seq(5, 2, cu, bound, "q", -1)
+    assert api._rows_per_seq(0, 2, cu, 0, "q", -1) == 0 and api._rows_per_seq(5, 2, cu, 3, "q", -1) == 3
