@@ -723,7 +723,7 @@ def _rows_per_seq(T, B, cu, max_seqlen, name, dev):
         raise ValueError("cu_seqlens must be a contiguous int32 [B + 1] on the current CUDA device")
     if max_seqlen is None:
         raise ValueError("packed rows need max_seqlen_q")
-    if T and max_seqlen < 1:
+    if T and B and max_seqlen < 1:
         raise ValueError(f"{name} has {T} rows, but max_seqlen_q is {max_seqlen}")
     return max_seqlen
 

@@ -47,4 +47,5 @@ def test_rows_but_a_bound_of_none_from_python():
     for bound in (0, -1):
         with pytest.raises(ValueError, match="max_seqlen_q"):
             api._rows_per_seq(5, 2, cu, bound, "q", -1)
+    assert api._rows_per_seq(5, 0, cu[:1], 0, "q", -1) == 0      # rows, but no sequences: nothing to do
     assert api._rows_per_seq(0, 2, cu, 0, "q", -1) == 0 and api._rows_per_seq(5, 2, cu, 3, "q", -1) == 3
