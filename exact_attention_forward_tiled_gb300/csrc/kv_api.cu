@@ -216,7 +216,8 @@ int attention(const void* q, const void* k_cache, const void* v_cache, const flo
   if (prefix_len > 0 && !prefix_pages) return FA_ERR_INVALID_ARG;
   if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(prefix_pages, 4)) return FA_ERR_ALIGNMENT;
-  if ((int64_t)prefix_len + (int64_t)max_pages * page_size + Sq > INT32_MAX) return FA_ERR_INVALID_ARG;
+  // positions are counted in 32 bits, up to the end of a tile that the last key begins
+  if ((int64_t)prefix_len + (int64_t)max_pages * page_size + Sq + 256 > INT32_MAX) return FA_ERR_INVALID_ARG;
   const int64_t G = Hq / Hk;
   if ((int64_t)total * Hq > INT32_MAX || (int64_t)Sq * G > INT32_MAX) return FA_ERR_INVALID_ARG;
 

@@ -421,8 +421,8 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const int* p
  * pages, quantised on the way if the cache is 8-bit.
  *
  *   k, v         16-bit [B * Sq, Hk, D], or packed [total_q, Hk, D] with
- *                cu_seqlens_q (Sq then bounds the rows of a sequence), by
- *                `strides`
+ *                cu_seqlens_q (Sq then bounds the rows of a sequence and is not
+ *                0 where there are rows), by `strides`
  *   seqlens_k    keys of each sequence WITH the new ones: row i of a sequence
  *                with n new rows goes to position seqlens_k[b] - n + i. A
  *                position below 0 is padding: the row is not written.
@@ -463,6 +463,7 @@ int fa_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, c
  *   Hq, Hk       Hq is a multiple of Hk; query head h reads K/V head
  *                h / (Hq / Hk)
  *   B            at most 4096 (FA_ERR_UNSUPPORTED beyond)
+ *   max_pages    prefix_len + max_pages * page_size + Sq is at most 2^31 - 257
  *   scale, causal   as fa_fwd (the mask is aligned to the bottom-right corner)
  *   workspace    device scratch of at least fa_fwd_kvcache_workspace_size
  *                bytes (prefix_len = 0), 256-byte aligned; its contents on
