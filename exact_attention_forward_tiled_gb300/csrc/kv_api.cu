@@ -103,7 +103,7 @@ struct Shape {
 // rows, 12 on average, 16-bit, D = 256: 133, 208 us).
 // Its work line holds kRowsMaxSeqs sequences; beyond, the few-row kernel does
 // it all.
-void choose(Pass& z, int64_t rows, int64_t mean, int Hk, int D, int elem_bytes, bool can_rows, int sms) {
+void choose(Pass& z, int64_t rows, int64_t mean, int B, int Hk, int D, int elem_bytes, bool can_rows, int sms) {
   z.rows = mean > (elem_bytes == 1 ? 32 : 16) && can_rows;
   z.qt = z.rows && rows > 128 && fa::rows_max_qt(D) == 2 ? 2 : 1;
   z.nb = rows <= 8 ? 1 : 2;
@@ -115,7 +115,7 @@ void choose(Pass& z, int64_t rows, int64_t mean, int Hk, int D, int elem_bytes, 
     const fa::KvAttnGeom g = fa::kv_attn_geom(D, elem_bytes, z.nb);
     z.rt = 8 * z.nb;
     z.unit = g.keys;
-    workers *= g.ctas * g.warps;
+    workers *= fa::kv_attn_ctas(D, elem_bytes, z.nb, B) * g.warps;
     per_cta = g.warps;
   }
   z.ranges = std::max(1, workers / Hk);
@@ -131,9 +131,9 @@ bool shape_of(Shape& z, int B, int Hq, int Hk, int S, int D, int elem_bytes, int
   // 32 rows 48 and 43, and with 100 own and 300 shared keys 19 and 15).
   z.split = prefix && rows_pre > 32;
   const bool one_line = prefix && !z.split;
-  choose(z.own, one_line ? rows_pre : rows_own, (rows_pre + B - 1) / B, Hk, D, elem_bytes,
+  choose(z.own, one_line ? rows_pre : rows_own, (rows_pre + B - 1) / B, B, Hk, D, elem_bytes,
          !one_line && B <= fa::kRowsMaxSeqs, sms);
-  choose(z.pre, rows_pre, rows_pre, Hk, D, elem_bytes, true, sms);
+  choose(z.pre, rows_pre, rows_pre, B, Hk, D, elem_bytes, true, sms);
   const int rt_pre = z.split ? z.pre.rt : z.own.rt;
   z.prefix_tiles = prefix ? (rows_pre + rt_pre - 1) / rt_pre : 0;
   z.own.whole = 2 * (int64_t)z.own.ranges;

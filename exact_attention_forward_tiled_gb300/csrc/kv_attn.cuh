@@ -104,6 +104,7 @@ struct KvCfg {
   static constexpr int kOffMisc = kOffBar + W * NS * 8;                    // abort flag, warp sums
   static constexpr int kOffCum = kOffMisc + 16 + 64;                       // cum[B + 1]
   static constexpr int kSmemFixed = kOffCum + 1024;
+  static_assert(kSmemFixed == kv_attn_smem(D, EB, NB), "shared memory of the geometry");
   static_assert(BOXES * (KT / 16) <= 32, "one lane per TMA box");
   static_assert(sizeof(KvSegment) <= 64, "segment slots");
   static_assert(NS >= 3 && CTAS * (kSmemFixed + 2048) <= 233472, "shared memory");

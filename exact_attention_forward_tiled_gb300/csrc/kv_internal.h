@@ -128,6 +128,22 @@ constexpr KvAttnGeom kv_attn_geom(int D, int elem_bytes, int nb) {
   return KvAttnGeom{ctas, warps, keys, slots};
 }
 
+// Shared memory of a CTA without the work line's sums (kv_attn.cuh lays it out),
+// and the CTAs that an SM holds with those of B sequences: two become one past
+// B = 2875 (D = 128, 8 bits) or 3643 (16 bits). The line is cut for those that
+// fit: cut for two, the second half of the grid started behind the first (B =
+// 3000 of 75 .. 300 keys, D = 128, e4m3: 393 us, 384 with this; B = 2800: 234).
+constexpr int kv_attn_smem(int D, int elem_bytes, int nb) {
+  const KvAttnGeom g = kv_attn_geom(D, elem_bytes, nb);
+  const int q = D * nb > 128 ? nb * D * 16 : 0;
+  const int scales = elem_bytes == 1 ? (g.slots <= 4 ? 2 : 4) * 2 * g.keys * 4 : 0;
+  return g.warps * (g.slots * (g.keys * D * elem_bytes + 8) + q + scales + 4 * 64) + 16 + 64 + 1024;
+}
+constexpr int kv_attn_ctas(int D, int elem_bytes, int nb, int B) {
+  const int ctas = kv_attn_geom(D, elem_bytes, nb).ctas;
+  return ctas == 2 && 2 * (kv_attn_smem(D, elem_bytes, nb) + (B + 1) * 4 + 1024) > 233472 ? 1 : ctas;
+}
+
 cudaError_t launch_kv_attn_d64(const KvAttnLaunch& L);
 cudaError_t launch_kv_attn_d128(const KvAttnLaunch& L);
 cudaError_t launch_kv_attn_d256(const KvAttnLaunch& L);

@@ -60,3 +60,16 @@ def test_sequences_that_overlap(kind, dtype, B, T, keys, P):
     assert api.fa_get_device_status(check=False)[0] == -6
     assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
     Case(22, [200, 37], [3, 1], 3, 3, 128, 16, kind, dtype).run()
+
+
+@pytest.mark.parametrize("kind,dtype,B", [(E4M3, BF16, 2900), (BF16, BF16, 3700), (I8, F16, 4096)])
+def test_batches_that_leave_one_cta_per_sm(kind, dtype, B):
+    """The sums of many sequences take the shared memory of a second CTA: the
+    line is cut for the CTAs that fit, so it has half as many ranges (of two
+    slots each in the workspace) and the results are right."""
+    c = Case(23, [(7 * i) % 37 for i in range(B)], [1] * B, 4, 2, 128, 16, kind, dtype)
+    out, lse = c.call()
+    api.fa_get_device_status()
+    c.check(out, lse, only=set(range(0, B, 13)) | {B - 1})
+    size = [api.fa_fwd_kvcache_workspace_size(b, 4, 2, 1, 128) for b in (2000, 4096)]
+    assert size[1] < 0.6 * size[0]
