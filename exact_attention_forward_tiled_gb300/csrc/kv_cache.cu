@@ -25,9 +25,8 @@
 // to int8 128 us, 6.3 TB/s, 93 % of a copy's rate; read from e4m3 to bf16
 // 122 us, 6.6 TB/s, 97 %.
 #include <cstdint>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
+#include "kv_codes.cuh"
 #include "kv_internal.h"
 #include "ptx.cuh"
 
@@ -37,32 +36,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;   // tokens of a CTA
-
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
-// four e4m3 codes -> two f16 pairs (exact)
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
-// four int8 codes -> two f16 pairs (exact): the byte c + 128 under the exponent
-// of 1024 is the f16 number 1024 + 128 + c; 1152 is taken off
-__device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-  const __half2 ha = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-  const __half2 hb = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-  lo = *reinterpret_cast<const uint32_t*>(&ha);
-  hi = *reinterpret_cast<const uint32_t*>(&hb);
-}
 
 // Row of the cache (page * page_size + offset) of row t, -1 where nothing is to
 // be done, -2 for a bad page entry. `append`: the rows are the last of their
@@ -157,7 +130,7 @@ __device__ __forceinline__ void dequantise(const uint2 (&c)[2], float scale, uin
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint32_t lo, hi;   // f16 pairs, exact
-      if (KIND == kCacheE4M3) e4m3x4_to_f16(cw[j], lo, hi); else i8x4_to_f16(cw[j], lo, hi);
+      codes_to_f16<KIND>(cw[j], lo, hi);
       const float2 a = unpack2<false>(lo), b = unpack2<false>(hi);
       float x0, x1, x2, x3;
       ptx::f2unpack(ptx::mul2(ptx::f2pack(a.x, a.y), s2), x0, x1);

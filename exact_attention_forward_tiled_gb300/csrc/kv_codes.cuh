@@ -1,5 +1,5 @@
-// Codes of 8-bit caches as f16 numbers, and shared-memory accesses of the
-// kernels that read a paged cache.
+// 16-bit elements and codes of 8-bit caches as numbers, and shared-memory
+// accesses of the kernels that read a paged cache.
 #pragma once
 
 #include <cstdint>
@@ -8,6 +8,13 @@
 #include "kv_internal.h"
 
 namespace fa {
+
+// two 16-bit elements of a word
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 
 // four codes of one word -> two f16 pairs, exact
 template <int KIND>

@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "kv_codes.cuh"
 #include "kv_internal.h"
 
 namespace fa {
@@ -34,11 +35,6 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if (BF16) {
