@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) kv_merge_kernel(const _
   if (w.bad || t < w.first || t >= w.first + w.n) return;
   const int hk = h / p.G, gq = h - hk * p.G;
   // (plain loads: the kernel before wrote it, perhaps while this one was resident)
-  const int own_U = p.cum[p.s.B], cum_b = p.cum[b];
+  const int own_U = p.cum[p.s.B];
 
   Partials own, pre{0, 0, 0, 0, 0, 0};
   int own_r, pre_r = 0;
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) kv_merge_kernel(const _
     const int R = (t - w.first) * p.G + gq;
     const int mt = R / rt;
     own_r = R - mt * rt;
-    own = partials_of(mp.own.pre_total + cum_b + mt * w.units, w.units, mp.own.ranges, mp.own.pre_total + own_U,
+    own = partials_of(mp.own.pre_total + p.cum[b] + mt * w.units, w.units, mp.own.ranges, mp.own.pre_total + own_U,
                       mp.own.whole + whole_slot(p, rt, b, w.first, mt));
     if (own.n == 1 && p.prefix_tiles == 0) return;   // finished by the worker that had all of it
   }
@@ -192,12 +192,13 @@ cudaError_t launch_kv_merge(const KvMergeParams& m, int D, cudaStream_t stream) 
   if (rows > 0x7fffffff) return cudaErrorInvalidValue;
   // Eight warps a row where few rows leave the machine empty and have many
   // partials each; one where there are so many rows that the CTAs' starts count.
-  // Whole calls, e4m3, 32 query and 8 K/V heads of 128, 4 warps against 8 and
-  // 16: 32 rows (8192 keys) 29.5, 18.9, 18.4 us; 256 rows 30.7, 29.0, 29.1; 512
-  // rows 22.8, 22.0, 26.3; 1024 rows 29.3, 32.3, 39.1. 4 warps against one: 1024
-  // rows 29.1, 30.6; 1536 rows 38.9, 37.4; 2048 rows 125.0, 123.0; 8192 rows
-  // 114.5, 103.3; 32000 rows (up to 30 keys) 80.0, 50.3; but 1152 rows of D = 256
-  // 132.8, 138.1.
+  // Whole calls, e4m3, 32 query and 8 K/V heads of 128, one, four and eight
+  // warps: 32 rows (8192 keys) 60.8, 28.1, 19.4 us; 256 rows 30.3, 23.3, 21.9; 512
+  // rows 21.4, 18.6, 17.9; 1024 rows 23.8, 22.5, 25.7; 1536 rows 35.4, 36.6, 40.0;
+  // 2048 rows 118.8, 121.1, 126.5; 8192 rows 97.8, 108.9, 130.5; 32000 rows (up to 30
+  // keys) 42.0, 71.8, 118.7. Heads of 256: 512 rows 66.0, 63.6, 62.8; 1152 rows
+  // 124.7, 123.1, 126.4; 1536 rows 158.6, 159.7, 163.2; 8192 rows 166.7, 177.5,
+  // 195.9. Heads of 64: 1536 rows 25.3, 25.4, 28.8.
   auto run = [&](auto one, auto four, auto eight) {
     if (rows >= 1536) return launch_early(one, (int)((rows + 3) / 4), 128, 0, stream, true, m);
     return rows > 512 ? launch_early(four, (int)rows, 128, 0, stream, true, m)
