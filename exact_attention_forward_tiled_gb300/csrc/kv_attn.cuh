@@ -46,7 +46,8 @@
 // of one), running ahead across items. (A range per CTA, its warps' partials
 // joined through shared memory, spent a third of its time on the barriers and
 // empty pipelines at the items' ends.) Measured: B = 64, 2048 .. 8192 keys, 32
-// query and 8 K/V heads of 128, e4m3: 116 us, 6.0 TB/s, 88 % of a copy's rate.
+// query and 8 K/V heads of 128, e4m3: 118 us alone, 5.9 TB/s, 86 % of a copy's
+// rate.
 //
 // Lane layout. The products' operand order along a contracted axis is free,
 // so it is chosen such that every shared-memory read is a 16-byte vector

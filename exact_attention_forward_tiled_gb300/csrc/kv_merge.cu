@@ -193,12 +193,12 @@ cudaError_t launch_kv_merge(const KvMergeParams& m, int D, cudaStream_t stream) 
   // Eight warps a row where few rows leave the machine empty and have many
   // partials each; one where there are so many rows that the CTAs' starts count.
   // Whole calls, e4m3, 32 query and 8 K/V heads of 128, one, four and eight
-  // warps: 32 rows (8192 keys) 60.8, 28.1, 19.4 us; 256 rows 30.3, 23.3, 21.9; 512
-  // rows 21.4, 18.6, 17.9; 1024 rows 23.8, 22.5, 25.7; 1536 rows 35.4, 36.6, 40.0;
-  // 2048 rows 118.8, 121.1, 126.5; 8192 rows 97.8, 108.9, 130.5; 32000 rows (up to 30
-  // keys) 42.0, 71.8, 118.7. Heads of 256: 512 rows 66.0, 63.6, 62.8; 1152 rows
-  // 124.7, 123.1, 126.4; 1536 rows 158.6, 159.7, 163.2; 8192 rows 166.7, 177.5,
-  // 195.9. Heads of 64: 1536 rows 25.3, 25.4, 28.8.
+  // warps: 32 rows (8192 keys) 61.0, 27.9, 16.7 us; 256 rows 30.4, 23.5, 22.1; 512
+  // rows 21.3, 18.6, 17.8; 1024 rows 24.1, 22.6, 25.7; 1536 rows 34.9, 36.2, 39.5;
+  // 2048 rows 117.4, 119.2, 124.9; 8192 rows 96.2, 107.7, 128.4; 32000 rows (up to
+  // 30 keys) 42.3, 72.2, 118.5. Heads of 256: 512 rows 65.7, 63.0, 62.1; 1152 rows
+  // 124.2, 122.4, 125.4; 1536 rows 157.2, 157.9, 161.8; 8192 rows 165.7, 176.2,
+  // 195.2. Heads of 64: 1536 rows 25.3, 24.7, 28.1; 8192 rows 64.1, 73.9, 90.4.
   auto run = [&](auto one, auto four, auto eight) {
     if (rows >= 1536) return launch_early(one, (int)((rows + 3) / 4), 128, 0, stream, true, m);
     return rows > 512 ? launch_early(four, (int)rows, 128, 0, stream, true, m)
